@@ -14,9 +14,9 @@
 //
 // All four products (the logits, the logits again, dx, dW) run on one kernel,
 // bound by the tensor cores and, in a loop, by the board's power: T = 8192, V =
-// 50257, d = 4096: 7.9 ms forward and backward, 1.70 PFLOP/s over the 8 T V d
+// 50257, d = 4096: 8.2 ms forward and backward, 1.65 PFLOP/s over the 8 T V d
 // issued (a plain bf16 product of cuBLAS in a loop: 1.71); T = 2047, V = 32003,
-// d = 1024: 0.36 ms, 1.49 PFLOP/s.  CTA pairs on 256 x 256 tiles (tcgen05.mma
+// d = 1024: 0.374 ms, 1.43 PFLOP/s.  CTA pairs on 256 x 256 tiles (tcgen05.mma
 // cta_group::2, fp32 accumulators in tensor memory, two of them so that a tile's
 // epilogue runs beside the next tile's products), operands by TMA into a
 // six-stage ring (a seventh stage, and clusters of two pairs that share B by
@@ -25,10 +25,14 @@
 //
 // The tensor cores truncate when they add into an accumulator, which biases a
 // long sum toward zero: over K = 2048 a logit is low by about 3e-6 of itself,
-// several times fp32's own error.  The forward therefore contracts 512 columns
-// at a time into alternating accumulators and its epilogue adds these parts in
-// registers (round to nearest).  In the backward that bias is far below the
-// bf16 rounding of dz and the sums run through.
+// several times fp32's own error.  The logits are therefore contracted 512
+// columns at a time into alternating accumulators and the epilogue adds these
+// parts in registers (round to nearest).  The backward forms its logits the same
+// way, so that they are the forward's bit for bit and their own error cancels in
+// z - lse: dz at the target is p - 1, in which an error of z is absolute (with
+// one accumulator through d = 4096 and a logit of 105, a token with 1 - p = 2e-5
+// got 1e-3).  dx and dW are sums of dz, already rounded to bf16, whose terms do
+// not cancel like that: they run through.
 #include <type_traits>
 
 #include "gemm_host.cuh"
@@ -47,9 +51,10 @@ using gemm::UMMA_K;
 constexpr int TILE = 256;          // rows and columns of a pair's tile
 constexpr int EPI_WARPS = 8;       // two per 32 rows: columns [0, 128) and [128, 256)
 constexpr int THREADS = 64 + 32 * EPI_WARPS;  // TMA warp, MMA warp, epilogue
-constexpr int SEG = 8;             // forward: K steps per accumulator
+constexpr int SEG = 8;             // logits: K steps per accumulator
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
+// 1 / kLog2e, the float, in two parts: what takes a base-2 maximum back exactly
+constexpr float kLn2 = 0.69314718246459961f, kLn2Lo = 7.3486932e-09f;
 
 enum Mode : int {
   LSE = 0,  // A = x (K = d), B = W: per-row partials of the log-sum-exp
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 1) vocab_gemm_kernel(const __grid_con
         constexpr int a_mn = decltype(kind)::value;
         const uint32_t a_lo0 = smem0 | desc_lead(a_mn), b_lo0 = (smem0 + (A_BYTES >> 4)) | desc_lead(b_mn);
         for (int ks = at.k0; ok && ks < at.k1; ++it) {
-          const int ke = MODE == LSE ? min(ks + SEG, at.k1) : at.k1;
+          const int ke = MODE == GRAD ? at.k1 : min(ks + SEG, at.k1);
           const int acc = it & 1;
           if (!ptx::mbar_wait_cluster_bounded(&tail->acc_empty[acc], ((it >> 1) & 1) ^ 1u, abort_flag,
                                               kWaitLimitNs)) {
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1) vocab_gemm_kernel(const __grid_con
     TileAt at{};
     for (int i = 0; ok && tile_of<MODE>(P, pair, i, at); ++i) {
       const Product& pr = MODE == GRAD && at.dw ? P.w : P.p;
-      const bool to_slab = MODE == GRAD && !at.dw && P.slab;
+      const bool to_slab = !at.dw && P.slab;
       const int out_rows = pr.rows, out_cols = pr.cols;
       const int row0 = at.m0 + rank * BM + q * 32, row = row0 + lane;
       const int col0 = at.n0 + half * 128;  // this warp's first column
@@ -455,19 +460,40 @@ __global__ void __launch_bounds__(THREADS, 1) vocab_gemm_kernel(const __grid_con
       const uint32_t lane_addr = (static_cast<uint32_t>(q * 32) << 16) + half * 128;
       // this row's constants, read while the products run
       int target = -1;
-      float base = 0.0f, mult = 0.0f, up = 0.0f;
+      float l = 0.0f, mult = 0.0f, up = 0.0f;
       if (MODE == LSE || MODE == DZ) {
         if (in) target = __ldg(P.targets + row);
         if (target >= P.V) target = -1;
         if (MODE == DZ && target >= 0) {
-          const float l = __ldg(P.lse + row);
+          l = __ldg(P.lse + row);
           up = __ldg(P.dloss + row) / scale;
-          base = l * kLog2e;
           mult = up * fmaf(2.0f * P.z_weight, l, 1.0f);
         }
         target = target < 0 ? -1 : target - (P.v0 + col0);  // column of this warp's, or outside
       }
-      if constexpr (MODE == LSE) {
+      // a chunk of 32 columns as bf16 into a 32 x 32 box (64-byte swizzle, two
+      // boxes in turn), out by TMA
+      auto store_box = [&](int c, auto value) {
+        uint8_t* box = reinterpret_cast<uint8_t*>(stg) + (stores & 1) * 2048;
+        if (stores >= 2) {
+          if (lane == 0) ptx::bulk_wait_read<1>();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 v = make_uint4(pack_bf16(value(8 * j), value(8 * j + 1)), pack_bf16(value(8 * j + 2), value(8 * j + 3)),
+                                     pack_bf16(value(8 * j + 4), value(8 * j + 5)), pack_bf16(value(8 * j + 6), value(8 * j + 7)));
+          *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = v;
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_3d(&pr.out, box, col0 + 32 * c, row0, 0);
+          ptx::bulk_commit();
+        }
+        ++stores;
+      };
+      if constexpr (MODE != GRAD) {
         const bool work = row0 < out_rows && ncol > 0;
         float z[128];
 #pragma unroll
@@ -493,6 +519,28 @@ __global__ void __launch_bounds__(THREADS, 1) vocab_gemm_kernel(const __grid_con
         }
         if (!ok) break;
         if (row0 >= out_rows) continue;
+        if constexpr (MODE == DZ) {
+          // dz: z - lse first (exact where they are close), then the exponential.
+          // Rows without a target and columns past the vocabulary are zero
+          // whatever their logits are.
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int e = 32 * c; e < 32 * c + 32; ++e) z[e] = mult * exp2_fast((z[e] - l) * kLog2e);
+            if (__any_sync(0xffffffffu, (unsigned)(target - 32 * c) < 32u)) {
+#pragma unroll
+              for (int e = 32 * c; e < 32 * c + 32; ++e)
+                if (target == e) z[e] -= up;
+            }
+            if (ncol < 32 * c + 32 || up == 0.0f) {
+#pragma unroll
+              for (int e = 32 * c; e < 32 * c + 32; ++e)
+                if (e >= ncol || up == 0.0f) z[e] = 0.0f;
+            }
+            store_box(c, [&](int e) { return z[32 * c + e]; });
+          }
+          continue;
+        }
         if (__any_sync(0xffffffffu, target >= 0 && target < ncol)) {
           float zt = 0.0f;
 #pragma unroll
@@ -525,8 +573,8 @@ __global__ void __launch_bounds__(THREADS, 1) vocab_gemm_kernel(const __grid_con
       }
       ++it;
       const uint32_t taddr = tmem_base + acc * BN + lane_addr;
-      if (row0 < out_rows && (ncol > 0 || MODE == DZ)) {
-        const int nch = MODE == DZ ? 4 : (ncol + 31) / 32;
+      if (row0 < out_rows && ncol > 0) {
+        const int nch = (ncol + 31) / 32;
         uint32_t r[2][32];
         ptx::tmem_ld32(taddr, r[0]);
         ptx::tmem_ld_wait(r[0]);
@@ -536,10 +584,8 @@ __global__ void __launch_bounds__(THREADS, 1) vocab_gemm_kernel(const __grid_con
           uint32_t(&cur)[32] = r[c & 1];
           uint32_t(&nxt)[32] = r[(c + 1) & 1];
           if (c + 1 < nch) ptx::tmem_ld32(taddr + 32 * (c + 1), nxt);
-          if (MODE != DZ) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) cur[e] = __float_as_uint(__uint_as_float(cur[e]) * scale);
-          }
+          for (int e = 0; e < 32; ++e) cur[e] = __float_as_uint(__uint_as_float(cur[e]) * scale);
           if (to_slab) {
             // fp32 share of dx: eight lanes per row through the staging buffer
             // (16-byte pieces XOR-swizzled by the row: no bank conflicts)
@@ -565,47 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) vocab_gemm_kernel(const __grid_con
               *p = v;
             }
           } else {
-            if (MODE == DZ) {
-              // dz of the chunk; rows without a target and columns past the
-              // vocabulary are zero whatever their logits are
-              const int left = ncol - 32 * c;
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                cur[e] = __float_as_uint(mult * exp2_fast(fmaf(__uint_as_float(cur[e]), kLog2e, -base)));
-              }
-              if (__any_sync(0xffffffffu, (unsigned)(target - 32 * c) < 32u)) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (target == 32 * c + e) cur[e] = __float_as_uint(__uint_as_float(cur[e]) - up);
-              }
-              if (left < 32 || up == 0.0f) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (e >= left || up == 0.0f) cur[e] = 0u;
-              }
-            }
-            // bf16 into a 32 x 32 box (64-byte swizzle, two boxes in turn), out
-            // by TMA
-            uint8_t* box = reinterpret_cast<uint8_t*>(stg) + (stores & 1) * 2048;
-            if (stores >= 2) {
-              if (lane == 0) ptx::bulk_wait_read<1>();
-              __syncwarp();
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint4 v = make_uint4(pack_bf16(__uint_as_float(cur[8 * j]), __uint_as_float(cur[8 * j + 1])),
-                                         pack_bf16(__uint_as_float(cur[8 * j + 2]), __uint_as_float(cur[8 * j + 3])),
-                                         pack_bf16(__uint_as_float(cur[8 * j + 4]), __uint_as_float(cur[8 * j + 5])),
-                                         pack_bf16(__uint_as_float(cur[8 * j + 6]), __uint_as_float(cur[8 * j + 7])));
-              *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = v;
-            }
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              ptx::tma_store_3d(&pr.out, box, col0 + 32 * c, row0, 0);
-              ptx::bulk_commit();
-            }
-            ++stores;
+            store_box(c, [&](int e) { return __uint_as_float(cur[e]); });
           }
           if (c + 1 < nch) ptx::tmem_ld_wait(nxt);
         }
@@ -907,7 +913,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int w = 1; w < 8; ++w) q[w - 1] = sh[w][r];
   join(q, 7);
-  const float l = (m + log2f(s)) * kLn2;
+  const float l = fmaf(m, kLn2, fmaf(m, kLn2Lo, log2f(s) * kLn2));  // one rounding at the size of l
   if (t >= V) record_status(status, MOE_ERR_DEVICE_BOUNDS);
   lse[row] = l;
   loss[row] = t >= 0 && t < V ? fmaf(z_weight * l, l, l - target) : 0.0f;
