@@ -578,7 +578,8 @@ MOE_API int moe_residual_norm_bwd(const void* dx, const void* dr_out, const void
 MOE_API int moe_embedding(const void* table, const int32_t* ids, int T, int V, int d, float scale, void* out,
                           void* stream);
 
-/* Workspace bytes of moe_embedding_bwd. */
+/* Workspace bytes of moe_embedding_bwd, for up to T tokens: a buffer sized for
+ * the longest batch serves every shorter one. */
 MOE_API int moe_embedding_workspace(int T, int V, int d, size_t* bytes);
 
 /* Gradient of the table: dtable[v,:] = scale * sum_{t: ids[t] = v} dout[t,:],

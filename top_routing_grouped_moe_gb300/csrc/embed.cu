@@ -24,6 +24,7 @@ constexpr int kSortPlaces = 8192;    // places of the placing warps: warps x ids
 constexpr int kChunkMax = 32;     // sorted rows per CTA of the sum
 constexpr int kAhead = 8;         // rows a thread has in flight
 constexpr int kSumThreads = 128;  // vectors of 8 columns per CTA of the sum
+constexpr int kFullCtas = 152;    // CTAs of the sum that leave no SM idle
 constexpr int kJoinGroups = 4;    // parts of a row's partials that a CTA of the join adds at once
 
 // Vector i of [T, nv]: token i / nv, four vectors per thread in flight.  Bound by
@@ -74,7 +75,7 @@ struct SortWs {
 // 1024, 23.8 us against 21.4).
 int chunk_of(int T, int nv) {
   const long long ctas = (long long)((T + kChunkMax - 1) / kChunkMax) * ((nv + kSumThreads - 1) / kSumThreads);
-  return ctas < 152 ? 8 : kChunkMax;
+  return ctas < kFullCtas ? 8 : kChunkMax;
 }
 int chunks_of(int T, int nv) { return (T + chunk_of(T, nv) - 1) / chunk_of(T, nv); }
 SortWs carve(void* ws, int T) {
@@ -396,9 +397,20 @@ __global__ void __launch_bounds__(kSumThreads* kJoinGroups)
 
 }  // namespace
 
-size_t embedding_ws_bytes(int T, int V, int d) {
-  (void)V;
+size_t embedding_ws_bytes(int T, int d) {
   return 2 * up256((size_t)T * 4) + 256 + up256((size_t)chunks_of(T, d / 8) * 2 * d * 4);
+}
+
+// Chunks of 8 need more partials than the chunks of 32 that follow them: the
+// most is at the longest batch that still has them (d = 2048: 2400 tokens 4.9
+// MB, 2401 tokens 1.3 MB).
+size_t embedding_ws_bytes_up_to(int T, int d) {
+  const int nv = d / 8;
+  const int short_ones = (kFullCtas - 1) / ((nv + kSumThreads - 1) / kSumThreads) * kChunkMax;  // chunk_of: 8 up to here
+  const int last = T < short_ones ? T : short_ones;
+  int chunks = chunks_of(T, nv);
+  if (last > 0 && chunks_of(last, nv) > chunks) chunks = chunks_of(last, nv);
+  return 2 * up256((size_t)T * 4) + 256 + up256((size_t)chunks * 2 * d * 4);
 }
 
 cudaError_t launch_embedding(const void* table, const int32_t* ids, int T, int V, int d, float scale, void* out,

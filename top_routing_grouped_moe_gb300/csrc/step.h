@@ -73,7 +73,9 @@ cudaError_t launch_residual_norm_bwd(const NormBwdArgs& a, bool r_f32, cudaStrea
 // ------------------------------------------------------------ token embedding
 cudaError_t launch_embedding(const void* table, const int32_t* ids, int T, int V, int d, float scale, void* out,
                              int* status, cudaStream_t s);
-size_t embedding_ws_bytes(int T, int V, int d);
+// what T tokens need, and the most that any batch of up to T tokens does
+size_t embedding_ws_bytes(int T, int d);
+size_t embedding_ws_bytes_up_to(int T, int d);
 cudaError_t launch_embedding_bwd(const void* dout, const int32_t* ids, int T, int V, int d, float scale,
                                  bool accumulate, void* dtable, void* ws, int* status, cudaStream_t s);
 

@@ -93,7 +93,7 @@ int moe_embedding_workspace(int T, int V, int d, size_t* bytes) {
   if (!bytes) return MOE_ERR_INVALID_ARG;
   int rc = check_embedding(T, V, d);
   if (rc) return rc;
-  *bytes = embedding_ws_bytes(T, V, d);
+  *bytes = embedding_ws_bytes_up_to(T, d);
   return MOE_OK;
 }
 
@@ -103,7 +103,7 @@ int moe_embedding_bwd(const void* dout, const int32_t* ids, int T, int V, int d,
   if (rc) return rc;
   if (!dout || !ids || !dtable || !all16(dout, dtable)) return MOE_ERR_INVALID_ARG;
   if (ws && !ws_ok(ws)) return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < embedding_ws_bytes(T, V, d)) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < embedding_ws_bytes(T, d)) return MOE_ERR_WORKSPACE;
   return done(launch_embedding_bwd(dout, ids, T, V, d, scale, accumulate != 0, dtable, ws, device_status_ptr(),
                                    st(stream)));
 }
