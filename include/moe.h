@@ -592,7 +592,8 @@ MOE_API int moe_embedding_bwd(const void* dout, const int32_t* ids, int T, int V
                               void* dtable, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of moe_cross_entropy (grad == 0), or of it and
- * moe_cross_entropy_bwd (grad != 0) with this `piece`. */
+ * moe_cross_entropy_bwd (grad != 0) with this `piece`, for up to T tokens: a
+ * buffer sized for the longest batch serves every shorter one. */
 MOE_API int moe_cross_entropy_workspace(int T, int d, int V, int piece, int grad, size_t* bytes);
 
 /* Softmax cross entropy of the vocabulary head, without the [T,V] logits in

@@ -98,6 +98,9 @@ struct VocabArgs {
 int vocab_piece(int T, int V, int piece);
 size_t vocab_fwd_ws_bytes(int T, int d, int V);
 size_t vocab_bwd_ws_bytes(int T, int d, int V, int piece);
+// the most that any batch of up to T tokens needs
+size_t vocab_fwd_ws_bytes_up_to(int T, int d, int V);
+size_t vocab_bwd_ws_bytes_up_to(int T, int d, int V, int piece);
 cudaError_t launch_cross_entropy(const VocabArgs& a, float* loss, float* lse, void* ws, int* status, cudaStream_t s);
 // dx [T, d], dW [V, d] bf16, each nullable
 cudaError_t launch_cross_entropy_bwd(const VocabArgs& a, const float* lse, const float* dloss, int piece, void* dx,

@@ -112,8 +112,8 @@ int moe_cross_entropy_workspace(int T, int d, int V, int piece, int grad, size_t
   if (!bytes || piece < 0) return MOE_ERR_INVALID_ARG;
   int rc = check_vocab(T, d, V);
   if (rc) return rc;
-  size_t b = vocab_fwd_ws_bytes(T, d, V);
-  const size_t g = grad ? vocab_bwd_ws_bytes(T, d, V, piece) : 0;
+  size_t b = vocab_fwd_ws_bytes_up_to(T, d, V);
+  const size_t g = grad ? vocab_bwd_ws_bytes_up_to(T, d, V, piece) : 0;
   *bytes = g > b ? g : b;
   return MOE_OK;
 }

@@ -1005,6 +1005,7 @@ cudaError_t launch_gemm(VParams& P, cudaStream_t s, const char* name) {
 // and its traffic.
 constexpr int kPairs = 76;  // of the 152-SM part
 constexpr int kTileSteps = 4;
+constexpr int kMaxSplits = 16;
 int late_rounds(int dx_steps, int dw_steps) { return cdiv_i(dx_steps + kTileSteps, dw_steps + kTileSteps); }
 double grad_steps(int T, int d, int piece, int s, bool dw) {
   const long long nx = (long long)cdiv_i(T, TILE) * cdiv_i(d, TILE) * s;
@@ -1018,7 +1019,7 @@ double grad_steps(int T, int d, int piece, int s, bool dw) {
 }
 int dx_splits(int T, int d, int piece, bool dw) {
   int best = 1;
-  for (int s = 2; s <= 16 && s * 8 <= cdiv_i(piece, BK); ++s)
+  for (int s = 2; s <= kMaxSplits && s * 8 <= cdiv_i(piece, BK); ++s)
     if (grad_steps(T, d, piece, s, dw) < grad_steps(T, d, piece, best, dw)) best = s;
   return best;
 }
@@ -1027,6 +1028,15 @@ struct BwdWs {
   size_t scale, dz, slab, total;
   int piece, pieces, splits;
 };
+// no batch of up to T tokens keeps more of dz
+size_t bwd_dz_limit(int T, int V, int piece_in) {
+  const long long all = (long long)cdiv_i(V, TILE) * TILE;
+  const long long cols = piece_in > 0 ? vocab_piece(T, V, piece_in) : all;
+  size_t n = (size_t)T * cols * 2;
+  const size_t limit = (size_t)1 << 30, narrow = (size_t)T * TILE * 2;
+  if (piece_in <= 0 && n > limit) n = narrow > limit ? narrow : limit;
+  return 256 + up256(n);
+}
 BwdWs bwd_ws(int T, int d, int V, int piece_in) {
   // (the same splits whether dW is wanted or not: the workspace's size and dx's
   // bits do not depend on it)
@@ -1095,6 +1105,40 @@ size_t vocab_fwd_ws_bytes(int T, int d, int V) {
   return up256((size_t)T * fwd_parts(T, V) * 8) + up256((size_t)T * 4);
 }
 size_t vocab_bwd_ws_bytes(int T, int d, int V, int piece) { return bwd_ws(T, d, V, piece).total; }
+
+// Few tokens keep four partials per CTA, more of them than the half tiles of
+// the other form: the most is at one of the two ends.
+size_t vocab_fwd_ws_bytes_up_to(int T, int d, int V) {
+  const size_t own = vocab_fwd_ws_bytes(T, d, V);
+  const size_t few = T > kFewTokens ? vocab_fwd_ws_bytes(kFewTokens, d, V) : 0;
+  return own > few ? own : few;
+}
+
+// dz grows with the tokens (up to a piece's limit), but dx's slabs come and go
+// with the splits.  Walks down the ranges of tokens in which the tiles and K
+// steps and the piece are constant.  Within one the slabs' cost in grad_steps
+// grows with the tokens, so the shortest batch has the most splits: its splits
+// with the longest batch's rows bound them all.  Ends when even the most splits
+// would not need more (8192 tokens: 30 us of host time, 65536: 400).
+size_t vocab_bwd_ws_bytes_up_to(int T, int d, int V, int piece_in) {
+  size_t most = 0;
+  for (int hi = T; hi >= 1;) {
+    const int piece = vocab_piece(hi, V, piece_in);
+    int lo = (hi - 1) / BK * BK + 1;  // BK divides TILE: one number of row tiles too
+    while (vocab_piece(lo, V, piece_in) != piece) ++lo;
+    const auto need = [&](int splits) {
+      const bool slabs = splits > 1 || piece < V;
+      return 256 + up256((size_t)hi * piece * 2) + (slabs ? up256((size_t)splits * hi * d * 4) : 0);
+    };
+    const size_t n = need(dx_splits(lo, d, piece, true));
+    if (n > most) most = n;
+    hi = lo - 1;
+    // below: no more dz than this (a piece is at most V rounded up, and its dz
+    // 1 GiB unless it is 256 columns or the caller's), no more slabs than kMaxSplits
+    if (hi >= 1 && bwd_dz_limit(hi, V, piece_in) + up256((size_t)kMaxSplits * hi * d * 4) <= most) break;
+  }
+  return most;
+}
 
 namespace {
 bool fill_logits(VParams& P, const VocabArgs& a, int v0, int nv) {
