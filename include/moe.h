@@ -610,7 +610,9 @@ MOE_API int moe_cross_entropy(const void* x, const void* W, const int32_t* targe
  * loss: 1/N for a mean; not read for ignored tokens):
  *   dz[t,v] = dloss[t] (exp(z - lse[t]) (1 + 2 z_weight lse[t]) - [v = targets[t]])
  *   dx = dz W  [T,d],   dW = dz^T x  [V,d]       bf16, either may be NULL
- * lse from moe_cross_entropy.  The vocabulary is taken `piece` columns at a
+ * lse from moe_cross_entropy.  An ignored token has dz = 0, whatever its
+ * logits; its row of x still enters the product dz^T x, so that a NaN or inf in
+ * it is a NaN in that channel of all of dW (0 * inf).  The vocabulary is taken `piece` columns at a
  * time (rounded down to a multiple of 256, at least 256; 0: as many as make dz
  * 1 GiB): the logits of a piece are computed again and dz kept in bf16 in the
  * workspace for the two products.  With several pieces dx is summed in fp32
