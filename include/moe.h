@@ -636,8 +636,8 @@ MOE_API int moe_grad_clip_workspace(int n, size_t* bytes);
  * outs[i] has grads[i]'s type and may be grads[i]; other overlaps are not
  * allowed.  outs NULL: the norm and the coefficient only.  norm, coef
  * (nullable): one fp32 each on the device.  The sum holds for elements of any
- * magnitude.  If the norm is not finite the gradients pass unscaled (coef 1)
- * and MOE_ERR_RANGE is recorded in the device status. */
+ * magnitude.  If the norm is not finite the gradients pass unscaled (coef 1,
+ * bit copies) and MOE_ERR_RANGE is recorded in the device status. */
 MOE_API int moe_grad_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types,
                           int n, float max_norm, float* norm, float* coef, void* ws, size_t ws_bytes, void* stream);
 

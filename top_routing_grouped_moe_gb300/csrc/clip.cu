@@ -229,8 +229,19 @@ __device__ __noinline__ void scale_elements(const char* in, char* out, int b0, i
   using E = Elem<TYPE>;
   for (int b = b0 + threadIdx.x * E::SIZE; b < b1; b += kThreads * E::SIZE) E::put(out + b, E::get(in + b) * coef);
 }
+// The same unscaled: the bits, as a product by 1 rewrites a NaN's.
+template <typename U>
+__device__ __noinline__ void copy_elements(const char* in, char* out, int b0, int b1) {
+  for (int b = b0 + threadIdx.x * (int)sizeof(U); b < b1; b += kThreads * (int)sizeof(U))
+    *reinterpret_cast<U*>(out + b) = *reinterpret_cast<const U*>(in + b);
+}
 __device__ __forceinline__ void scale_range(const Piece& q, int b0, int b1, float coef) {
   if (b0 >= b1) return;
+  if (coef == 1.0f) {
+    if (q.type == MOE_GRAD_F32) copy_elements<uint32_t>(q.p, q.out, b0, b1);
+    else copy_elements<uint16_t>(q.p, q.out, b0, b1);
+    return;
+  }
   if (q.type == MOE_GRAD_BF16) scale_elements<MOE_GRAD_BF16>(q.p, q.out, b0, b1, coef);
   else if (q.type == MOE_GRAD_F32) scale_elements<MOE_GRAD_F32>(q.p, q.out, b0, b1, coef);
   else scale_elements<MOE_GRAD_F16>(q.p, q.out, b0, b1, coef);
@@ -269,7 +280,7 @@ __device__ __forceinline__ void scale_chunk(const Piece& q, Vecs& v, float coef)
     return;
   }
   uint4* out = reinterpret_cast<uint4*>(q.out + v.head);
-  if (coef != 1.0f) {  // 1: bit copies (a NaN's bits too)
+  if (coef != 1.0f) {  // 1: bit copies
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       if (q.type == MOE_GRAD_BF16) scale_vec<MOE_GRAD_BF16>(v.raw[j], coef);
