@@ -75,7 +75,7 @@ def _kernel_sources(kernel: str):
     elif kernel.startswith("vocab"):
         files = _GEMM_COMMON + ["vocab.cu", "step.h"]
     elif kernel.startswith("embedding"):
-        files = ["embed.cu", "step.h", "common.cuh", "internal.h"]
+        files = ["embed.cu", "step.h", "ptx.cuh", "common.cuh", "internal.h"]
     elif kernel.startswith("residual_norm"):
         files = ["norm.cu", "step.h", "ptx.cuh", "common.cuh", "internal.h"]
     elif kernel in ("grad_squares", "grad_scale"):
