@@ -383,7 +383,18 @@ def moe_residual_norm_bwd(dx, dr_out, o, gate, gate_kind, w_post, w_pre, r_out, 
                  T, d, r_f32, alpha, dr, d_o, dgate, dw_post, dw_pre, ws, ws_bytes, stream)
 
 
+def _index(name, t, T):
+    """Token ids and targets: their usual torch type is int64 and their usual
+    form a slice of a batch, both of which would be read as other ids."""
+    if isinstance(t, torch.Tensor):
+        if t.dtype is not torch.int32:
+            raise TypeError(f"{name}: int32 (given {t.dtype})")
+        if not t.is_contiguous() or t.numel() < T:
+            raise ValueError(f"{name}: {T} of them, contiguous")
+
+
 def moe_embedding(table, ids, T, V, d, scale, out, stream=None):
+    _index("ids", ids, T)
     return _call("moe_embedding", table, ids, T, V, d, scale, out, stream)
 
 
@@ -392,6 +403,7 @@ def moe_embedding_workspace(T, V, d) -> int:
 
 
 def moe_embedding_bwd(dout, ids, T, V, d, scale, accumulate, dtable, ws, ws_bytes, stream=None):
+    _index("ids", ids, T)
     return _call("moe_embedding_bwd", dout, ids, T, V, d, scale, accumulate, dtable, ws, ws_bytes, stream)
 
 
@@ -400,10 +412,12 @@ def moe_cross_entropy_workspace(T, d, V, piece=0, grad=True) -> int:
 
 
 def moe_cross_entropy(x, W, targets, T, d, V, z_weight, loss, lse, ws, ws_bytes, stream=None):
+    _index("targets", targets, T)
     return _call("moe_cross_entropy", x, W, targets, T, d, V, z_weight, loss, lse, ws, ws_bytes, stream)
 
 
 def moe_cross_entropy_bwd(x, W, targets, lse, dloss, T, d, V, z_weight, piece, dx, dW, ws, ws_bytes, stream=None):
+    _index("targets", targets, T)
     return _call("moe_cross_entropy_bwd", x, W, targets, lse, dloss, T, d, V, z_weight, piece, dx, dW, ws, ws_bytes,
                  stream)
 

@@ -82,7 +82,8 @@ class MoELM:
         return {n: p[f"{i}.{n}"] for n in names if f"{i}.{n}" in p}
 
     def forward(self, ids, targets, p, stream=None):
-        """Per-token losses [T] fp32 (0 where the target is negative).  A padding
+        """Per-token losses [T] fp32 (0 where the target is negative), for ids
+        and targets [T] int32, contiguous (another type is refused).  A padding
         token (negative id) needs a negative target: its row is zero, whose norm
         has a gain of 1/sqrt(eps) per block in the backward, and a gradient of
         that size would take the range of the layer's fp16 gradient terms from
