@@ -35,3 +35,11 @@ def test_slices_of_a_batch_and_short_ones(L, call):
     for ids in (batch[:, 1:], batch.t(), torch.zeros(2 * T, dtype=torch.int32)[::2], torch.zeros(T - 1, dtype=torch.int32)):
         with pytest.raises(ValueError):
             CALLS[call](L, ids)
+
+
+def test_gradients_on_the_host(L):
+    """A list of their addresses would be read by the GPU."""
+    g = torch.ones(8)
+    for outs in (None, [g], [torch.empty(8)]):
+        with pytest.raises(ValueError):
+            L.GradList([g], outs)

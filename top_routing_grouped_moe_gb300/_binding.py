@@ -424,8 +424,9 @@ def moe_cross_entropy_bwd(x, W, targets, lse, dloss, T, d, V, z_weight, piece, d
 
 class GradList:
     """The host arrays of moe_grad_clip for a list of contiguous gradient
-    tensors (bf16, fp32 or fp16), laid out once: `grads`, and `outs` (None: the
-    norm only; grads itself: in place) with the same types and sizes."""
+    tensors (bf16, fp32 or fp16) of one GPU, laid out once: `grads`, and `outs`
+    (None: the norm only; grads itself: in place) with the same types and
+    sizes."""
 
     _TYPES = {torch.bfloat16: MOE_GRAD_BF16, torch.float32: MOE_GRAD_F32, torch.float16: MOE_GRAD_F16}
 
@@ -433,12 +434,17 @@ class GradList:
         grads, outs = list(grads), None if outs is None else list(outs)
         if not grads or (outs is not None and len(outs) != len(grads)):
             raise ValueError("GradList: one output for each of at least one gradient")
+        dev = grads[0].device
+        if dev.type != "cuda":
+            raise ValueError(f"GradList: gradients on {dev}")
         for i, g in enumerate(grads):
             if g.dtype not in self._TYPES:
                 raise TypeError(f"GradList: gradient {i} has type {g.dtype}")
             for t in (g,) if outs is None else (g, outs[i]):
                 if t.dtype != g.dtype or t.numel() != g.numel() or not t.is_contiguous():
                     raise ValueError(f"GradList: gradient {i} and its output are contiguous, of one type and size")
+                if t.device != dev:
+                    raise ValueError(f"GradList: gradient {i} and its output are on {dev} like the first one")
         n = self.n = len(grads)
         self.tensors = (grads, outs)  # the addresses below stay valid
         self.grads = (_P * n)(*[t.data_ptr() for t in grads])
