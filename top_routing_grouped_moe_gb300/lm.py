@@ -107,17 +107,18 @@ class MoELM:
         head = "table" if self.tied else "head"
         B.moe_cross_entropy_bwd(self.x[-1], p[head], targets, self.lse, dloss, T, d, V, self.z_weight, 0, self.dx,
                                 g[head], ws, n, stream)
+        dx = self.dx  # gradient of the normed input, from the head and then from each layer's own buffer
         up = None  # gradient of the residual stream from the blocks above
         for i in reversed(range(self.blocks)):
             layer, dr = self.layers[i], self.dr[i & 1]
-            B.moe_residual_norm_bwd(self.dx, up, layer.y, None, B.MOE_GATE_NONE, p[f"{i}.w_post"],
+            B.moe_residual_norm_bwd(dx, up, layer.y, None, B.MOE_GATE_NONE, p[f"{i}.w_post"],
                                     p[f"{i + 1}.w_pre"], self.r[i + 1], self.rstd_post[i], self.rstd_pre[i + 1], T, d,
                                     False, self.r_scale, dr, self.dy, None, g[f"{i}.w_post"], g[f"{i + 1}.w_pre"], ws,
                                     n, stream)
-            self.dx = layer.backward(self.x[i], self.dy, self._layer_weights(p, i), stream=stream)
+            dx = layer.backward(self.x[i], self.dy, self._layer_weights(p, i), stream=stream)
             up = dr
         dr = self.dr[self.blocks & 1]
-        B.moe_residual_norm_bwd(self.dx, up, None, None, B.MOE_GATE_NONE, None, p["0.w_pre"], self.r[0], None,
+        B.moe_residual_norm_bwd(dx, up, None, None, B.MOE_GATE_NONE, None, p["0.w_pre"], self.r[0], None,
                                 self.rstd_pre[0], T, d, False, 1.0, dr, None, None, None, g["0.w_pre"], ws, n, stream)
         B.moe_embedding_bwd(dr, ids, T, V, d, self.scale, self.tied, g["table"], ws, n, stream)
         return g
