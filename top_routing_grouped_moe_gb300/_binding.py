@@ -434,17 +434,17 @@ class GradList:
         grads, outs = list(grads), None if outs is None else list(outs)
         if not grads or (outs is not None and len(outs) != len(grads)):
             raise ValueError("GradList: one output for each of at least one gradient")
-        dev = grads[0].device
-        if dev.type != "cuda":
-            raise ValueError(f"GradList: gradients on {dev}")
+        gpu = grads[0].get_device()  # -1: on the host
+        if gpu < 0:
+            raise ValueError(f"GradList: gradients on {grads[0].device}")
         for i, g in enumerate(grads):
             if g.dtype not in self._TYPES:
                 raise TypeError(f"GradList: gradient {i} has type {g.dtype}")
-            for t in (g,) if outs is None else (g, outs[i]):
-                if t.dtype != g.dtype or t.numel() != g.numel() or not t.is_contiguous():
-                    raise ValueError(f"GradList: gradient {i} and its output are contiguous, of one type and size")
-                if t.device != dev:
-                    raise ValueError(f"GradList: gradient {i} and its output are on {dev} like the first one")
+            o = g if outs is None else outs[i]
+            if o is not g and (o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous()
+                               or o.get_device() != gpu) or not g.is_contiguous() or g.get_device() != gpu:
+                raise ValueError(f"GradList: gradient {i} and its output are contiguous, of one type and size, on the "
+                                 "GPU of the first one")
         n = self.n = len(grads)
         self.tensors = (grads, outs)  # the addresses below stay valid
         self.grads = (_P * n)(*[t.data_ptr() for t in grads])
