@@ -519,7 +519,9 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
 // one), an SM as many CTAs as fit kBwdThreads, which share its shared memory for
 // their rings: while one waits at its barrier another computes.  T = 16384, d =
 // 2048: two CTAs of 256 threads 67 us, one of 512 70, three 76, four 90
-// (registers); T = 16384, d = 1280: three of 160 47, one of 480 49, two 55.
+// (registers); T = 16384, d = 1280: three of 160 47, one of 480 49, two 55.  Two
+// vectors per thread spill 84 to 132 bytes (128 registers): T = 8192, d = 8192:
+// 173 us, 0.69 of the copy rate (fp32 stream 243, 0.73), d = 4096: 70, 0.85.
 BwdPlan plan_of(int d, bool r_f32) {
   BwdPlan L;
   const int nv = d / 8;

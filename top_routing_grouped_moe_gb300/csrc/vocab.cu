@@ -14,9 +14,9 @@
 //
 // All four products (the logits, the logits again, dx, dW) run on one kernel,
 // bound by the tensor cores and, in a loop, by the board's power: T = 8192, V =
-// 50257, d = 4096: 8.2 ms forward and backward, 1.65 PFLOP/s over the 8 T V d
+// 50257, d = 4096: 8.1 ms forward and backward, 1.67 PFLOP/s over the 8 T V d
 // issued (a plain bf16 product of cuBLAS in a loop: 1.71); T = 2047, V = 32003,
-// d = 1024: 0.374 ms, 1.43 PFLOP/s.  CTA pairs on 256 x 256 tiles (tcgen05.mma
+// d = 1024: 0.373 ms, 1.44 PFLOP/s.  CTA pairs on 256 x 256 tiles (tcgen05.mma
 // cta_group::2, fp32 accumulators in tensor memory, two of them so that a tile's
 // epilogue runs beside the next tile's products), operands by TMA into a
 // six-stage ring (a seventh stage, and clusters of two pairs that share B by
